@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
           break;
         }
         last = c;
-        const float pc = sm.pc[c], qc = sm.qc[c];
-        if (!prob_ok(pc) || !prob_ok(qc)) {
+        const float pc = sm.pc[c], qc = sm.qc[c], uc = sm.u[c];
+        if (!prob_ok(pc) || !prob_ok(qc) || !(uc >= 0.f && uc < 1.f)) {
           bad |= PA_FLAG_PROB;
           action = kBadLane;
           break;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         if (!with_q)
           for (int k = 0; k < n_rej; ++k)
             if (sm.gone[k] == sm.tok[c]) rx = 0.0;
-        if ((double)sm.u[c] * mass * (double)qc < rx) {
+        if ((double)uc * mass * (double)qc < rx) {
           cur = c;
           ++count;
           if (lane == 0) sm.path[count] = c;

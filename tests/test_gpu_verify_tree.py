@@ -302,3 +302,30 @@ def test_minus_zero_is_zero(drafts):
         assert flags == 0
         res.append(got)
     same(*res)
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("x", [-0.1, 1.0, 2.5, np.nan, np.inf, -np.inf])
+def test_a_random_number_outside_its_range(x, drafts):
+    """u_accept outside [0, 1): the lane is refused where the walk comes to that node, and takes no
+    notice of it where it does not."""
+    trees = [sh.chain(4), [-1, 0, 0, 1], sh.chain(4)]
+    p, q, tokens, u, us = make(2, trees, 100)
+    q = q if drafts else None
+    u[:], u[5] = 0.5, 1 - 2.0 ** -24
+    p[4, tokens[5]] = 0  # node 1 of the second lane is tried and never kept: node 3 is not reached
+    good, flags = run(p, q, tokens, trees, u, us)
+    assert flags == 0 and 3 not in good[1][4:8]
+    away = u.copy()
+    away[[0, 4, 7]] = x  # roots' numbers are not read, node 3's is not used
+    got, flags = run(p, q, tokens, trees, away, us)
+    assert flags == 0
+    same(got, good)
+    bad = u.copy()
+    bad[5] = x
+    got, flags = run(p, q, tokens, trees, bad, us)
+    assert flags == pa.FLAGS["PROB"]
+    assert got[0][1] == -1 and (got[1][4:8] == -1).all() and (got[2][4:8] == -1).all()
+    for b in (0, 2):
+        same([got[0][b], got[1][4 * b:4 * b + 4], got[2][4 * b:4 * b + 4]],
+             [good[0][b], good[1][4 * b:4 * b + 4], good[2][4 * b:4 * b + 4]])
