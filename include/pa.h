@@ -543,8 +543,8 @@ pa_status pa_attention_tree(const void* q, const void* k_cache, const void* v_ca
  *                 NULL where drafts were chosen, not drawn
  *   draft_tokens  int32 [T], the nodes' tokens (node 0's is not read)
  *   tree_parents  as above; here node 0 is the only root
- *   u_accept      fp32 [T], u_accept[t] in [0, 1) decides on node t (not read
- *                 for nodes that the walk does not come to)
+ *   u_accept      fp32 [T], u_accept[t] in [0, 1) decides on node t (of no
+ *                 matter for nodes that the walk does not come to)
  *   u_sample      fp32 [B] in [0, 1), the draw of the following token
  *   n_accepted    int32 [B]: drafted nodes kept (0 .. q_len - 1), -1 for a lane
  *                 without rows or not verified
@@ -564,10 +564,15 @@ pa_status pa_attention_tree(const void* q, const void* k_cache, const void* v_ca
  * token has the target's distribution.
  *
  * Sums are exact to about 2^-50 of a row, and a lane's results do not depend
- * on the other lanes or on the step. A tree that is none raises PA_FLAG_TREE; rows read that hold a value
- * outside [0, 2), sum to 2 or more or to under 2^-40, a u_sample and a used
- * u_accept outside [0, 1) raise PA_FLAG_PROB; the lane's outputs are then -1. 1 <= max_q_len <=
- * PA_TREE_MAX_NODES; vocab <= 2^24.
+ * on the other lanes or on the step. A tree that is none raises PA_FLAG_TREE.
+ * Rows read, the target's or the draft's, that hold a value outside [0, 2) or
+ * sum to 2 or more (found from 1.99 on) or to under 2^-40, a u_sample and a used
+ * u_accept outside [0, 1) raise PA_FLAG_PROB; the lane's outputs are then -1.
+ * (Read are the target's row that the following token is drawn from and, with
+ * draft_probs, both rows of every node one of whose children is rejected.)
+ * A lane of more than max_q_len rows raises PA_FLAG_HOST_BOUND: its n_accepted
+ * is -1, its path and tokens are left as they are.
+ * 1 <= max_q_len <= PA_TREE_MAX_NODES; vocab <= 2^24.
  */
 pa_status pa_verify_tree(const float* target_probs, const float* draft_probs,
                          const int32_t* draft_tokens, const int32_t* tree_parents,

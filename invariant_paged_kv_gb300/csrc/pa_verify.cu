@@ -71,6 +71,11 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 __device__ __forceinline__ u64 warp_incl(u64 v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -101,11 +106,11 @@ struct Shared {
   int bad;
   u64 runs[kRuns];
   u64 wsum[kWarps];  // sums of the CTA's warps
-  float fsum[kWarps];
+  float fsum[kWarps], qsum[kWarps];  // of the target's entries, of the draft's
   int wbad;          // whether it met a value that is no probability
   // by pass parity: what every CTA of the cluster left here
   u64 csum[2][kMaxCluster];
-  float cfsum[2][kMaxCluster];
+  float cfsum[2][kMaxCluster], cqsum[2][kMaxCluster];
   int cbad[2][kMaxCluster];
 };
 
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
     Sums sums;
     sums.start();
     uint32_t top = 0;          // largest bit pattern met: a negative value or NaN is large
-    uint64_t psum = f32x2(0.f, 0.f);
+    uint64_t psum = f32x2(0.f, 0.f), qsum = psum;
     const int g0 = gw * iters * 32 + lane;
     const float ah = sm.ah, al = sm.al;
     // kRej: rejections, 2 standing for more
@@ -371,6 +376,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
 #pragma unroll
           for (int j = 0; j < 4; ++j) top = max(top, max(__float_as_uint(h[j]), __float_as_uint(q[j])));
           psum = add_f32x2(psum, add_f32x2(f32x2(h[0], h[1]), f32x2(h[2], h[3])));
+          if constexpr (kRej >= 1) qsum = add_f32x2(qsum, add_f32x2(f32x2(q[0], q[1]), f32x2(q[2], q[3])));
           if constexpr (kRej == 1) {  // A = 1
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -417,42 +423,44 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
                  prob_ok(qv.y) && prob_ok(qv.z) && prob_ok(qv.w));
       }
     }
-    float fs, fs1;
+    float fs, fs1, qs, qs1;
     f32x2_split(psum, fs, fs1);
-    fs += fs1;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) fs += __shfl_xor_sync(0xffffffffu, fs, o);
+    f32x2_split(qsum, qs, qs1);
+    fs = warp_sum_f(fs + fs1);
+    qs = warp_sum_f(qs + qs1);
     if (lane == 0) {
       sm.wsum[warp] = total_w;
       sm.fsum[warp] = fs;
+      sm.qsum[warp] = qs;
     }
     if (__syncthreads_or(bad)) sm.wbad = 1;  // the same value from every thread
     if (pass == 0) cluster.barrier_wait();
     if (warp == 0) {
       // its sums to every CTA of the cluster (the barrier makes them seen)
       const u64 all = warp_sum(lane < kWarps ? sm.wsum[lane] : 0);
-      float f = lane < kWarps ? sm.fsum[lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+      const float f = warp_sum_f(lane < kWarps ? sm.fsum[lane] : 0.f);
+      const float q = warp_sum_f(lane < kWarps ? sm.qsum[lane] : 0.f);
       __syncwarp();
       if (lane < ranks) {
         Shared* o = cluster.map_shared_rank(&sm, lane);
         o->csum[par][rank] = all;
         o->cfsum[par][rank] = f;
+        o->cqsum[par][rank] = q;
         o->cbad[par][rank] = sm.wbad;
       }
     }
     cluster.sync();
     const u64 mine = lane < ranks ? sm.csum[par][lane] : 0;
-    float fall = lane < ranks ? sm.cfsum[par][lane] : 0.f;
+    const float fall = warp_sum_f(lane < ranks ? sm.cfsum[par][lane] : 0.f);
+    const float qall = warp_sum_f(lane < ranks ? sm.cqsum[par][lane] : 0.f);
     int badall = lane < ranks ? sm.cbad[par][lane] : 0;
     const u64 incl = warp_incl(mine, lane);
     const u64 total = __shfl_sync(0xffffffffu, incl, 31);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) fall += __shfl_xor_sync(0xffffffffu, fall, o);
-    // rows that hold a value outside [0, 2) or sum to 2 or more are no
-    // probabilities (and would not fit the fixed point)
-    badall = __any_sync(0xffffffffu, badall) || !(fall < 1.99f);
+    // rows that hold a value outside [0, 2), sum to 2 or more (and would not fit
+    // the fixed point; the floats' sum, within 2^-13, is held against 1.99) or to
+    // next to nothing are no probabilities
+    auto no_row = [](float sum) -> bool { return !(sum < 1.99f && sum >= 0x1p-40f); };
+    badall = __any_sync(0xffffffffu, badall) || no_row(fall) || (use_q && no_row(qall));
     const bool empty = total < kNothing;
     if (badall || (empty && n_rej == 0)) {
       __syncthreads();

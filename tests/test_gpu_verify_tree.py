@@ -329,3 +329,38 @@ def test_a_random_number_outside_its_range(x, drafts):
     for b in (0, 2):
         same([got[0][b], got[1][4 * b:4 * b + 4], got[2][4 * b:4 * b + 4]],
              [good[0][b], good[1][4 * b:4 * b + 4], good[2][4 * b:4 * b + 4]])
+
+
+@pytest.mark.parametrize("children", [1, 3])
+def test_rows_that_are_no_distribution(children):
+    """A row that is read and sums to nothing, or to 2 and more, refuses the lane, a draft row as a
+    target row; one that is not read does not."""
+    V = 257
+    trees = [[-1] + [0] * children] * 3
+    n = children + 1
+    p, q, tokens, u, us = make(3, trees, V)
+    u[:] = 0.5
+    p[n, tokens[n + 1:2 * n]] = 0  # the second lane rejects every child: both its rows are read
+    good, flags = run(p, q, tokens, trees, u, us)
+    assert flags == 0 and good[0][1] == 0
+    one = lambda value: np.eye(1, V, 200, dtype=np.float32)[0] * np.float32(value)  # noqa: E731
+
+    def case(which, row, flag):
+        a, b = p.copy(), q.copy()
+        (a if which == "p" else b)[row[0]] = row[1]
+        got, flags = run(a, b, tokens, trees, u, us)
+        assert flags == flag, (which, flags)
+        if flag:
+            assert got[0][1] == -1 and (got[1][n:2 * n] == -1).all() and (got[2][n:2 * n] == -1).all()
+            for i in (0, 2):
+                same([got[0][i], got[1][i * n:i * n + n], got[2][i * n:i * n + n]],
+                     [good[0][i], good[1][i * n:i * n + n], good[2][i * n:i * n + n]])
+        else:
+            same(got, good)
+
+    full = np.full(V, 2.0 / (V - children), np.float32) * np.float32(1 + 2.0 ** -10)
+    full[tokens[n + 1:2 * n]] = 0
+    for which in "pq":
+        for row in (np.zeros(V, np.float32), one(2.0 ** -42), full, 4 * full, 40 * full):
+            case(which, (n, row), pa.FLAGS["PROB"])
+        case(which, (n + 1, np.zeros(V, np.float32)), 0)  # a row that no walk comes to
