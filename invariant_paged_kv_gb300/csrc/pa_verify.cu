@@ -20,7 +20,7 @@
 // only, and must not depend on the batch. FP64 would do but runs at 2
 // operations per clock and SM here. A thread adds its entries in three floats
 // (Sums below): the rounding error of every addition is known exactly and
-// added to the next float, which leaves less than 2^-50 of a row behind.
+// added to the next float, which leaves less than V 2^-58 of a row behind.
 // Threads' sums then become 64-bit integers in units of 2^-62, exact and
 // associative, and so do the entries of the one run of the vocabulary that
 // the draw ends in. Which thread adds what depends on the vocabulary alone.
@@ -32,8 +32,8 @@
 // memory. A row is read once per pass (the draw's second look at one 128-entry
 // run comes out of L2), and a lane's passes follow one another: the lanes with
 // the most rejections bound a batch. 64 trees of 16 nodes, vocabulary 248320:
-// 75 us, 142 MB over all passes (1.9 TB/s, about 5 us a pass); 24 trees of 25
-// chosen drafts, vocabulary 100003, one pass each: 13.5 us; one chain,
+// 81 us, 142 MB over all passes (1.8 TB/s, about 5 us a pass); 24 trees of 25
+// chosen drafts, vocabulary 100003, one pass each: 13.7 us; one chain,
 // vocabulary 32000: 7.7 us. 16 CTAs a lane or 512 threads were no faster.
 #include <cooperative_groups.h>
 
@@ -138,39 +138,60 @@ __device__ __forceinline__ long long to_fix_signed(float x) {
   return x < 0.f ? -m : m;
 }
 
-// Sums of up to 2^13 non-negative values of total under 2, two at a time. s1
-// holds 4 + the sum, so its last place is 2^-21 and every value and partial
-// sum is smaller than it: t = s1 + h rounds, and h - (t - s1) is what it lost,
-// exactly. That goes to s2 (1.5 2^-8 + the sum: last place 2^-31, losses under
-// 2^-22 each), and what s2 loses to s3, with the low parts.
+// Sums of non-negative values of total under 2, two at a time. s1 holds 4 + the
+// sum, so its last place is 2^-21 and every value and partial sum is smaller than
+// it: t = s1 + h rounds, and h - (t - s1) is what it lost, exactly. That goes to
+// s2, and what s2 loses to s3. Those two hold a bias of their own and stay in its
+// binade over the few values between two calls of take(), so what they gathered
+// is the difference of their bits, in whole last places (2^-40 and 2^-58). The
+// only error is s3's, 2^-59 for each value added: V 2^-58 of a row at the worst,
+// 2^-40 for 248320 entries. (With no integer behind them, s3 without a bias, it
+// was 2^-46 there and 2^-32 for 2^24 entries, on ordinary rows.)
 struct Sums {
+  static constexpr float kBias2 = 0x1.8p-17f, kBias3 = 0x1.8p-35f;
   uint64_t s1, s2, s3;
+  long long low;  // taken out of s2 and s3, in units of 2^-58
   __device__ __forceinline__ void start() {
     s1 = f32x2(4.f, 4.f);
-    s2 = f32x2(0x1.8p-8f, 0x1.8p-8f);
-    s3 = f32x2(0.f, 0.f);
+    s2 = f32x2(kBias2, kBias2);
+    s3 = f32x2(kBias3, kBias3);
+    low = 0;
   }
   __device__ __forceinline__ void add(uint64_t h) {
     const uint64_t neg = f32x2(-1.f, -1.f);
     const uint64_t t = add_f32x2(s1, h);
-    const uint64_t e = fma_f32x2(fma_f32x2(s1, neg, t), neg, h);
+    add_low(fma_f32x2(fma_f32x2(s1, neg, t), neg, h));
     s1 = t;
-    const uint64_t t2 = add_f32x2(s2, e);
-    s3 = add_f32x2(s3, fma_f32x2(fma_f32x2(s2, neg, t2), neg, e));
-    s2 = t2;
+  }
+  // (values up to 2^-22)
+  __device__ __forceinline__ void add_low(uint64_t e) {
+    const uint64_t neg = f32x2(-1.f, -1.f);
+    const uint64_t t = add_f32x2(s2, e);
+    s3 = add_f32x2(s3, fma_f32x2(fma_f32x2(s2, neg, t), neg, e));
+    s2 = t;
+  }
+  // after every 8 calls of add and 8 of add_low: s2 is within 2^-18 of its bias
+  // (8 2^-22, the low parts 2^-23 in all), s3 within 2^-36 (16 2^-41)
+  __device__ __forceinline__ void take() {
+    low += (long long)places(s2, kBias2) * (1 << 18) + places(s3, kBias3);
+    s2 = f32x2(kBias2, kBias2);
+    s3 = f32x2(kBias3, kBias3);
+  }
+  __device__ __forceinline__ static int places(uint64_t s, float bias) {
+    float a, b;
+    f32x2_split(s, a, b);
+    return (int)(__float_as_uint(a) + __float_as_uint(b) - 2 * __float_as_uint(bias));
   }
   __device__ __forceinline__ long long total() const {
-    float a, b, c, d, e, f;
+    float a, b;
     f32x2_split(s1, a, b);
-    f32x2_split(s2, c, d);
-    f32x2_split(s3, e, f);
-    return to_fix_signed(a - 4.f) + to_fix_signed(b - 4.f) + to_fix_signed(c - 0x1.8p-8f) +
-           to_fix_signed(d - 0x1.8p-8f) + to_fix_signed(e) + to_fix_signed(f);
+    return low * 16 + (to_fix_signed(a - 4.f) + to_fix_signed(b - 4.f));
   }
 };
 
 // max(h - A q, 0) as h + l, A = ah + al. Where it is positive, h >= A q makes
-// the loss of the difference exact.
+// the loss of the difference exact; A, its product and the loss less the
+// product's low part each round by 2^-49 of h: 2^-47 of it in all.
 __device__ __forceinline__ void less_pair(float& h, float& l, float ah, float al, float q) {
   const float ph = ah * q;
   const float pl = fmaf(al, q, fmaf(ah, q, -ph));
@@ -390,9 +411,12 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
           }
           sums.add(f32x2(h[0], h[1]));
           sums.add(f32x2(h[2], h[3]));
-          if constexpr (kRej >= 1)
-            sums.s3 = add_f32x2(sums.s3, add_f32x2(f32x2(l[0], l[1]), f32x2(l[2], l[3])));
+          if constexpr (kRej >= 1) {
+            sums.add_low(f32x2(l[0], l[1]));
+            sums.add_low(f32x2(l[2], l[3]));
+          }
         }
+        sums.take();
       }
     };
     if (!use_q)
@@ -540,8 +564,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         const u64 rb = (2 * lane + 1) * per_run < iters ? sm.runs[2 * lane + 1] : 0;
         const u64 in = warp_incl(ra + rb, lane);
         unsigned hits = __ballot_sync(0xffffffffu, base + in > t);
-        // the slice's own sum may end 2^-50 short of the threads': then the
-        // last run that holds anything
+        // the slice's own sum, of entries cut to 2^-62, may end short of the
+        // threads': then the last run that holds anything
         const unsigned held = __ballot_sync(0xffffffffu, ra + rb > 0);
         if (!hits) hits = held ? 0x80000000u >> __clz(held) : 1u;
         const int s2 = __ffs(hits) - 1;

@@ -364,3 +364,65 @@ def test_rows_that_are_no_distribution(children):
         for row in (np.zeros(V, np.float32), one(2.0 ** -42), full, 4 * full, 40 * full):
             case(which, (n, row), pa.FLAGS["PROB"])
         case(which, (n + 1, np.zeros(V, np.float32)), 0)  # a row that no walk comes to
+
+
+def border_row(rng, V, drafts):
+    """A row (with a draft row whose only drawn token is always rejected), u_sample = k / 2^24 and the
+    token that follows, by whole numbers: the residual's entries are multiples of 2^-58, and u_sample
+    times their sum lies within a few of these units of a running sum."""
+    unit = 2.0 ** 58
+    while True:
+        x = rng.normal(size=V) * 2.0
+        p = np.exp(x - x.max())
+        p = (p / p.sum()).astype(np.float32)
+        p = (np.rint(p.astype(np.float64) * unit) / unit).astype(np.float32)  # (fewer bits, so exact)
+        q = np.zeros(V, np.float32)
+        if drafts:
+            q = p[rng.permutation(V)] * np.float32(0.9)
+            q = (np.rint(q.astype(np.float64) * unit) / unit).astype(np.float32)
+        z = V - 1
+        p[z], q[z] = 0.0, 2.0 ** -12
+        fine = 5
+        p[fine], q[fine] = 2.0 ** 23 / unit, 0.0
+        whole = lambda a: np.rint(a.astype(np.float64) * unit).astype(np.int64)  # noqa: E731
+        k = int(rng.integers(1 << 21, 1 << 22))
+        r = np.maximum(whole(p) - whole(q), 0)
+        cum = np.cumsum(r)
+        at = int(np.searchsorted(cum, (k * int(cum[-1])) >> 24, side="right"))
+        if not 100 < at < V - 100:
+            continue
+        # off the entry what the running sum there has beyond u_sample times the whole, first coarsely
+        # (a float's last place), then by an entry small enough to hold any whole number of units
+        q[at] = 0.0
+        for place, want in ((at, 0), (fine, int(rng.integers(-3, 4)))):
+            r = np.maximum(whole(p) - whole(q), 0)
+            cum = np.cumsum(r)
+            gap = (int(cum[at]) << 24) - k * int(cum[-1])  # in 2^-24 units; (1 - u) of a change reaches it
+            p[place] = (int(r[place]) + round((want * 2 ** 24 - gap) / (2 ** 24 - k))) / unit
+            if not p[place] > 0:
+                break
+        r = np.maximum(whole(p) - whole(q), 0)
+        cum = np.cumsum(r)
+        gap = (int(cum[at]) << 24) - k * int(cum[-1])
+        if p[at] <= 0 or not 0 < p[fine] < 2.0 ** -34 or abs(gap) > 8 << 24:
+            continue
+        y = int(np.searchsorted(cum, (k * int(cum[-1])) >> 24, side="right"))
+        return p, q, z, np.float32(k / 2 ** 24), y
+
+
+@pytest.mark.parametrize("drafts", [False, True])
+@pytest.mark.parametrize("V,lanes", [(2049, 16), (100003, 16), (248320, 12), (1 << 24, 4)])
+def test_draws_within_a_hair_of_a_running_sum(V, lanes, drafts):
+    """Sums of rows keep what their entries hold: a draw that misses a running sum by 2^-57 of a row
+    falls on the right side of it, up to the largest vocabulary."""
+    rng = np.random.default_rng(V + drafts)
+    rows = [border_row(rng, V, drafts) for _ in range(lanes)]
+    trees = [[-1, 0] if drafts else [-1]] * lanes
+    n = len(trees[0])
+    p = np.repeat(np.stack([r[0] for r in rows]), n, 0)
+    q = np.repeat(np.stack([r[1] for r in rows]), n, 0) if drafts else None
+    tokens = np.repeat(np.array([r[2] for r in rows], np.int32), n)
+    got, flags = run(p, q, tokens, trees, np.full(n * lanes, 0.5, np.float32),
+                     np.array([r[3] for r in rows], np.float32))
+    assert flags == 0 and (got[0] == 0).all()
+    np.testing.assert_array_equal(got[2][::n], [r[4] for r in rows])
