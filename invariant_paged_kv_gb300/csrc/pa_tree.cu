@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(kFoldWarps * 32) tree_fold_kernel(const TreePa
   const int cu0 = p.cu_seqlens[b];
   const long long base = ((long long)info.y << 32) | (uint32_t)info.x;
   const int ns = info.w, rows = info.z * p.H;
-  // (after a wait that ran out, a lane's entry may be what the workspace held:
-  // nothing out of bounds is touched for it)
+  // (an entry outside the call's bounds is none, and nothing is touched for it)
   if (ns < 2 || ns > PA_TREE_MAX_SPLITS || info.z < 0 || info.z > p.max_q_len || cu0 < 0 ||
       (long long)cu0 + info.z > p.T || base < 0 || base > p.capacity - (long long)info.z * ns)
     return;

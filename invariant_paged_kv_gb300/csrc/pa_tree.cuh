@@ -193,6 +193,16 @@ struct TreeWalk {
     return true;
   }
 
+  // The reporting warp, at its end: the windows that it has not come to (it may
+  // leave early, when a wait runs out), so that the fold finds every lane's entry.
+  __device__ __forceinline__ void finish(const TreeParams& p, int lane) {
+    while (cls == 0 && b0 + 32 < p.B) {
+      pairs0 += win_pairs;
+      b0 += 32;
+      window(p, lane, true);
+    }
+  }
+
   // Split of the thread's lane that `item` belongs to, and the item's index
   // among the split's (kv head, row tile) pairs.
   __device__ __forceinline__ void item_of(const TreeParams& p, long long item, int& split, int& rest) const {

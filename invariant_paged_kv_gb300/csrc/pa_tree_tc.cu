@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok) break;
       n_ring += 2 * it.nkt;
     }
+    if (!vs && blockIdx.x == 0) walk.finish(p, lane);
     if (!vs) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   } else if (warp == 6) {
     // ------------------------- look over the tree tiles ----------------------

@@ -406,3 +406,37 @@ def test_loose_bounds_change_nothing(dtype):
     for q_len, ctx in ((9, 5000), (256, 605), (256, 1 << 17)):
         got, flags = s.run(dev, max_q_len=q_len, max_ctx_len=ctx)
         assert flags == 0 and torch.equal(got, want), (q_len, ctx)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_a_wait_that_runs_out_leaves_the_other_lanes(dtype):
+    """The CTA that leaves the fold its entries gives up in the first of two windows of lanes, over a
+    workspace in which an earlier step had other lanes (more nodes, more splits): every lane that it
+    does not work on has its ordinary bits all the same, the split ones too."""
+    old = sh.Step([(900, sh.chain(5))] * 40, 8, 2, 128, 16, dtype, seed=30)
+    s = sh.Step([(1500, sh.chain(32))] + [(700, sh.chain(2)), (40, sh.chain(3))] * 22, 8, 2, 128, 16, dtype, seed=31)
+    dev, kw = s.to_device(), s.kwargs()
+    want, flags = s.run(dev)
+    assert flags == 0
+    need = [pa.tree_workspace_bytes(x.B, x.T, max(x.n), int(x.ctx.max()), 8, 2, 128, 16, x.kind) for x in (old, s)]
+    # what the earlier step leaves where this one keeps its entries: theirs, of other lanes
+    ws = torch.zeros(max(need), dtype=torch.uint8, device="cuda")
+    entries = torch.zeros(len(ws) // 16, 4, dtype=torch.int32, device="cuda")
+    entries[:, 2], entries[:, 3] = 5, 2
+    ws[:entries.numel() * 4] = entries.view(torch.uint8).view(-1)
+    out, st, L = torch.zeros_like(dev["q"]), pa.new_status(), pa.load()
+    args = [dev[k] for k in ("q", "k_cache", "v_cache", "block_tables", "cu_seqlens_q", "ctx_lens", "tree_parents")]
+    try:
+        L.pa_test_set_wait_cycles(2_000_000)  # about a millisecond of SM clock
+        L.pa_test_skip_split_item(0)
+        pa.attention_tree(*args, out, workspace=ws, status=st, **kw)
+        flags = pa.read_status(st)
+    finally:
+        L.pa_test_skip_split_item(-1)
+        L.pa_test_set_wait_cycles(0)
+    assert flags == pa.FLAGS["TIMEOUT"], f"flags {flags:#x}"
+    assert not torch.equal(out[:32], want[:32])  # the lane of the item that was given up
+    bad = [b for b in range(1, s.B) if not torch.equal(out[s.cu[b]:s.cu[b + 1]], want[s.cu[b]:s.cu[b + 1]])]
+    assert not bad, bad
+    pa.attention_tree(*args, out, workspace=ws, status=st, **kw)
+    assert pa.read_status(st) == 0 and torch.equal(out, want)
