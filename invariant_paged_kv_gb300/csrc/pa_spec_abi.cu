@@ -1,5 +1,6 @@
 // C ABI of the speculative decoding operators: host-side validation and
 // launch sequencing. Declarations and contracts are in include/pa.h.
+#include <cfloat>
 #include <cstring>
 
 #include "pa_host.cuh"
@@ -23,6 +24,13 @@ namespace {
 
 // Shortest split of a lane's keys (tree_split_len).
 int tree_split0(pa_dtype dtype) { return dtype == PA_F32 ? 128 : 256; }
+
+// A factor of scores as a float that is neither 0 nor infinite: a hidden key's
+// score of -inf times 0, or a score of 0 times infinity, would be NaN.
+float tree_score_scale(double x) {
+  const float f = (float)x;
+  return f < FLT_TRUE_MIN ? FLT_TRUE_MIN : f > FLT_MAX ? FLT_MAX : f;
+}
 
 // (node, head) pairs of a row tile.
 int tile_pairs_of(pa_dtype dtype, int32_t max_q_len, int32_t g) {
@@ -231,7 +239,7 @@ pa_status pa_attention_tree(const void* q, const void* k_cache, const void* v_ca
   p.tile_rows = pairs / g;
   p.split0 = tree_split0(dtype);
   p.grow = f32 ? 0 : 1;  // fp32 is bound by FMA: short splits spread it over the SMs
-  p.scale_log2 = scale * 1.4426950408889634f * (fp8 ? k_scale : 1.f);
+  p.scale_log2 = tree_score_scale((double)scale * 1.4426950408889634 * (fp8 ? (double)k_scale : 1.0));
   p.v_scale = fp8 ? v_scale : 1.f;
   p.wait_cycles = wait_cycles();
   p.skip_item = test_skip_item();

@@ -685,7 +685,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       float c2 = p.scale_log2;
       if constexpr (FP8) {
         const int e = valid ? p.q_exp[row * p.H + head] : 127;
-        c2 *= __uint_as_float((uint32_t)(e - 7) << 23);  // 2^(exponent - 7)
+        // 2^(exponent - 7); neither 0 nor infinite, as the scale itself (a row of
+        // zeros, whose exponent is the smallest, under a small scale)
+        c2 = fminf(fmaxf(c2 * __uint_as_float((uint32_t)(e - 7) << 23), FLT_TRUE_MIN), FLT_MAX);
       }
       float m = -INFINITY, l = 0.f;
       bool ok = true;

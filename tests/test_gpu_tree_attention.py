@@ -440,3 +440,20 @@ def test_a_wait_that_runs_out_leaves_the_other_lanes(dtype):
     assert not bad, bad
     pa.attention_tree(*args, out, workspace=ws, status=st, **kw)
     assert pa.read_status(st) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype,scale,k_scale", [
+    ("fp8", None, 1e-12), ("fp8", None, 1e-30), ("fp8", 1e-30, 1e-20), ("fp8", 1e-12, 1e-30), ("fp8", 3e38, 1e-38),
+    ("bf16", 1e-45, 1.0), ("bf16", 3e38, 1.0), ("f32", 1e-45, 1.0), ("f32", 3e38, 1.0)])
+def test_scales_of_any_size(dtype, scale, k_scale):
+    """Every finite positive scale, rows of zeros among them: a score is never 0 times infinity."""
+    s = sh.Step([(300, [-1, 0, 0, 1]), (1300, sh.chain(5)), (20, sh.chain(70))], 8, 2, 128, 16, dtype, seed=17)
+    s.k_scale = float(np.float32(k_scale))
+    if scale is not None:
+        s.scale = float(np.float32(scale))
+    if scale == 3e38 and dtype != "fp8":
+        s.k.mul_(0.0)  # (NaN past the lanes' ends stays)
+    s.q[::2] = 0
+    out, flags = s.run()
+    assert flags == 0
+    s.check(out)
