@@ -898,9 +898,10 @@ __global__ void __launch_bounds__(256) tree_q_pieces_kernel(const TreeParams p) 
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   // times 2^(7 - exponent of the largest element); the score scale takes it
-  // back (rows of zeros or infinities: the nearest exponent in range)
+  // back. Rows of next to nothing take the smallest exponent whose factor has a
+  // place in fp32 with room to spare, rows with an infinity the largest finite one
   int e = (int)(__float_as_uint(mx) >> 23);
-  e = min(max(e, 20), 240);
+  e = min(max(e, 20), 254);
   const float up = __uint_as_float((uint32_t)(127 + 7 - (e - 127)) << 23);
   uint32_t hi = 0, lo = 0;
 #pragma unroll

@@ -457,3 +457,27 @@ def test_scales_of_any_size(dtype, scale, k_scale):
     out, flags = s.run()
     assert flags == 0
     s.check(out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+def test_queries_near_the_largest(dtype):
+    """Elements around 2^116 to 2^120 under a scale that brings the scores back to ordinary size."""
+    s = sh.Step([(300, sh.chain(8)), (1300, sh.chain(5))], 8, 2, 128, 16, dtype, seed=16)
+    s.q = (s.q.float() * 2.0 ** 116).to(s.q.dtype)
+    s.q[3, :, 5], s.q[3, :, 6] = 2.0 ** 118, 2.0 ** 120
+    s.q[10, :, 7] = -2.0 ** 119
+    s.scale = float(np.float32(2.0 ** -116 / np.sqrt(128)))
+    out, flags = s.run()
+    assert flags == 0
+    s.check(out)
+
+
+def test_keys_of_zeros_under_any_scale():
+    """The largest q and a large scale over codes of zero: every score is 0."""
+    s = sh.Step([(300, [-1, 0, 0, 1]), (1300, sh.chain(5))], 8, 2, 128, 16, "fp8", seed=18)
+    s.k[s.k != 0x7F] = 0
+    s.q[1, :, 3] = 3e38
+    s.k_scale, s.scale = 4096.0, 1.0
+    out, flags = s.run()
+    assert flags == 0
+    s.check(out)
