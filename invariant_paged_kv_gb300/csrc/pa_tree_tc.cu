@@ -898,10 +898,10 @@ __global__ void __launch_bounds__(256) tree_q_pieces_kernel(const TreeParams p) 
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   // times 2^(7 - exponent of the largest element); the score scale takes it
-  // back. Rows of next to nothing take the smallest exponent whose factor has a
-  // place in fp32 with room to spare, rows with an infinity the largest finite one
+  // back (both factors are normal from 8 to 254: rows under 2^-119 take 8, rows
+  // with an infinity 254)
   int e = (int)(__float_as_uint(mx) >> 23);
-  e = min(max(e, 20), 254);
+  e = min(max(e, 8), 254);
   const float up = __uint_as_float((uint32_t)(127 + 7 - (e - 127)) << 23);
   uint32_t hi = 0, lo = 0;
 #pragma unroll

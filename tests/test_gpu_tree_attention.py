@@ -481,3 +481,15 @@ def test_keys_of_zeros_under_any_scale():
     out, flags = s.run()
     assert flags == 0
     s.check(out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+def test_queries_near_the_smallest(dtype):
+    """Elements around 2^-122 under a scale that brings the scores up to ordinary size."""
+    s = sh.Step([(300, sh.chain(8)), (1300, sh.chain(5))], 8, 2, 128, 16, dtype, seed=16)
+    s.q = (s.q.float() * 2.0 ** -122).to(s.q.dtype)
+    s.q[3, :, 5] = 2.0 ** -118
+    s.scale = float(np.float32(2.0 ** 122 / np.sqrt(128)))
+    out, flags = s.run()
+    assert flags == 0
+    s.check(out)
