@@ -111,21 +111,33 @@ __device__ __forceinline__ float v_elem(const TreeParams& p, long long slot, int
 }
 
 // (rare) Add the values that P V left out because they are not finite -- of
-// the nodes in badw that the row attends -- to what the row has stored. A call
-// of its own, so that its code stays out of the way.
+// the nodes in badw that the row attends -- to what the row has stored. Any
+// weight leaves an infinity or NaN what it is, but one of 0 (with m the row's
+// maximum) makes NaN of an infinity, as the product makes of a cache key's. A
+// call of its own, so that its code stays out of the way.
 template <int D, bool FP8>
 __device__ __noinline__ void tree_add_bad(const TreeParams& p, int lane_b, int kvh, int past, int node,
                                           const int* par, const uint32_t* badw, bool single,
-                                          size_t out_at, long long entry) {
+                                          size_t out_at, long long entry, float m) {
   const int* table = p.block_tables + (size_t)lane_b * p.max_blocks;
   for (int a = node; a >= 0;) {
     if ((badw[a >> 5] >> (a & 31)) & 1u) {
       const int key = past + a;
       int blk = table[key / p.bs];
       blk = blk < 0 || blk >= p.NB ? 0 : blk;
+      const long long slot = (long long)blk * p.bs + key % p.bs;
+      bool nothing = false;
+      if (!FP8) {  // (e4m3 codes have no infinity)
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + out_at;
+        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k_cache) + ((size_t)slot * p.Hkv + kvh) * D;
+        float s = 0.f;
+        for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
+        nothing = ex2_approx(s * p.scale_log2 - m) == 0.f;
+      }
       for (int d = 0; d < D; ++d) {
-        const float v = v_elem<D, FP8>(p, (long long)blk * p.bs + key % p.bs, kvh, d);
+        float v = v_elem<D, FP8>(p, slot, kvh, d);
         if (isfinite(v)) continue;
+        if (nothing) v = NAN;
         if (single) {
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + out_at + d;
           *o = __float2bfloat16_rn(__bfloat162float(*o) + v);
@@ -823,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (valid) tree_emit<D>(p, ov, c, single, inv, (row * p.H + head) * D, e);
         }
         if (any_bad && valid)
-          tree_add_bad<D, FP8>(p, it.lane, it.kvh, past, node, par, badw, single, (row * p.H + head) * D, e);
+          tree_add_bad<D, FP8>(p, it.lane, it.kvh, past, node, par, badw, single, (row * p.H + head) * D, e, m);
       }
       tc_fence_before();
       n_ring += 2 * it.nkt;

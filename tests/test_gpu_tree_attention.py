@@ -493,3 +493,29 @@ def test_queries_near_the_smallest(dtype):
     out, flags = s.run()
     assert flags == 0
     s.check(out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("past", [40, 1500])
+@pytest.mark.parametrize("low", [-float("inf"), -1e4])
+def test_an_infinity_of_weight_zero_is_nan(dtype, past, low):
+    """0 times infinity, as for a key of the cache, not infinity: a node's V whose weight is nothing."""
+    s = sh.Step([(past, [-1, 0, 0, 1, 2]), (past, sh.chain(40))], 8, 2, 64, 16, dtype, seed=2)
+    s.q[..., 0] = 1.0
+    for b, j in ((0, 1), (1, 2)):
+        i, r = s.row(b, past + j)
+        s.k[i, r] = 0.0
+        s.k[i, r, :, 0] = low * 8
+    clean, flags = s.run()
+    assert flags == 0
+    s.check(clean)
+    for b, j, value in ((0, 1, float("inf")), (0, 2, -float("inf")), (1, 2, -float("inf"))):
+        i, r = s.row(b, past + j)
+        s.v[i, r, 0, 7] = value
+    got, flags = s.run()
+    assert flags == 0
+    want = clean.clone()
+    want[[1, 3], :4, 7] = float("nan")   # node 1 and its child: weight 0
+    want[[2, 4], :4, 7] = -float("inf")  # node 2 and its child: an ordinary weight
+    want[5 + 2:, :4, 7] = float("nan")
+    assert torch.equal(torch.nan_to_num(got, nan=12345.0), torch.nan_to_num(want, nan=12345.0))
