@@ -212,7 +212,6 @@ pa_status pa_attention_tree(const void* q, const void* k_cache, const void* v_ca
                             v_scale, status, stream);
     if (st != PA_OK) return st;
   }
-  if (max_q_len == 0) return PA_OK;
 
   TreeParams p;
   std::memset(&p, 0, sizeof(p));
@@ -255,7 +254,8 @@ pa_status pa_attention_tree(const void* q, const void* k_cache, const void* v_ca
     p.acc = reinterpret_cast<float*>(ws + L.acc);
   }
   const long long tiles = (max_q_len + p.tile_rows - 1) / p.tile_rows;
-  const long long items = (long long)B * Hkv * (ns > 0 ? ns : 1) * tiles;  // at most
+  // at most; with max_q_len 0 one CTA says that the lanes' rows exceed it
+  const long long items = max_q_len ? (long long)B * Hkv * (ns > 0 ? ns : 1) * tiles : 1;
   cudaError_t e;
   if (f32) {
     const long long most = 4LL * num_sms();
@@ -285,7 +285,7 @@ pa_status pa_attention_tree(const void* q, const void* k_cache, const void* v_ca
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
   count_launches(1);
-  if (L.pairs) {
+  if (L.pairs && max_q_len) {
     if (launch_tree_fold(p, f32, s) != cudaSuccess) return PA_ERR_CUDA;
     count_launches(1);
   }

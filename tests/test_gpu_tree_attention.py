@@ -519,3 +519,14 @@ def test_an_infinity_of_weight_zero_is_nan(dtype, past, low):
     want[[2, 4], :4, 7] = -float("inf")  # node 2 and its child: an ordinary weight
     want[5 + 2:, :4, 7] = float("nan")
     assert torch.equal(torch.nan_to_num(got, nan=12345.0), torch.nan_to_num(want, nan=12345.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("ctx", [0, 100, 2000])
+def test_a_bound_of_no_rows_is_raised(dtype, ctx):
+    """max_q_len = 0 with lanes that have rows: every one exceeds it, which is said; nothing is written
+    but the new K/V rows."""
+    s = sh.Step([(30, sh.chain(3)), (1400, sh.chain(5))], 8, 2, 64, 16, dtype, seed=1)
+    out, flags = s.run(max_q_len=0, max_ctx_len=ctx)
+    assert flags == pa.FLAGS["HOST_BOUND"]
+    assert torch.isnan(out).all()
