@@ -590,7 +590,8 @@ pa_status pa_verify_tree(const float* target_probs, const float* draft_probs,
  *                       [num_blocks, block_size, Hkv, D] (16-byte aligned)
  *   ctx_lens            int32 [B] of the step (its nodes included)
  *   path, n_accepted    as pa_verify_tree leaves them
- *   new_ctx_lens        int32 [B], not ctx_lens itself: ctx - q_len + 1 +
+ *   new_ctx_lens        int32 [B], apart from the inputs (memory shared with one
+ *                       of them returns PA_ERR_INVALID_ARG): ctx - q_len + 1 +
  *                       n_accepted, the keys that remain; ctx - q_len for a
  *                       lane whose n_accepted is negative, ctx for one
  *                       without rows

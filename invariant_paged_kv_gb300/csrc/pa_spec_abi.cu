@@ -125,6 +125,12 @@ bool encode_tree_pieces_map(CUtensorMap* map, const void* q, int T, int H, int D
 
 bool aligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
 
+// Whether two arrays share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 pa_status check_caches(void* const* k, void* const* v, int32_t layers) {
   for (int32_t i = 0; i < layers; ++i)
     if (!k[i] || !v[i] || !aligned16(k[i]) || !aligned16(v[i])) return PA_ERR_INVALID_ARG;
@@ -345,7 +351,16 @@ pa_status pa_compact_kv(void* const* k_caches, void* const* v_caches, int32_t la
   if (T > 0 && B == 0) return PA_ERR_INVALID_ARG;
   if (B == 0 || layers == 0) return layers == 0 && B > 0 ? PA_ERR_INVALID_ARG : PA_OK;
   if (!k_caches || !v_caches || !block_tables || !cu_seqlens_q || !ctx_lens || !path ||
-      !n_accepted || !new_ctx_lens || max_blocks_per_seq <= 0 || new_ctx_lens == ctx_lens)
+      !n_accepted || !new_ctx_lens || max_blocks_per_seq <= 0)
+    return PA_ERR_INVALID_ARG;
+  // several CTAs, and the launches of further layers, read a lane's lengths and
+  // path after one of them has written its new length
+  const size_t i32 = sizeof(int32_t), new_bytes = (size_t)B * i32;
+  if (overlap(new_ctx_lens, new_bytes, ctx_lens, (size_t)B * i32) ||
+      overlap(new_ctx_lens, new_bytes, cu_seqlens_q, ((size_t)B + 1) * i32) ||
+      overlap(new_ctx_lens, new_bytes, path, (size_t)T * i32) ||
+      overlap(new_ctx_lens, new_bytes, n_accepted, (size_t)B * i32) ||
+      overlap(new_ctx_lens, new_bytes, block_tables, (size_t)B * max_blocks_per_seq * i32))
     return PA_ERR_INVALID_ARG;
   st = check_caches(k_caches, v_caches, layers);
   if (st != PA_OK) return st;

@@ -158,3 +158,15 @@ def test_binding_wants_the_write_whole(lib, given):
     with pytest.raises(ValueError, match="go together"):
         pa.attention_tree(q, kc, kc.clone(), i(1, 4), i(2), i(1), i(3), q.clone(), max_q_len=3, max_ctx_len=9,
                           scale=0.1, workspace=torch.zeros(256, dtype=torch.uint8), **{k: new[k] for k in given})
+
+
+def test_compact_wants_its_output_apart(lib):
+    """new_ctx_lens over any part of an input is refused: the kernel's CTAs would read what another wrote."""
+    arr = (ctypes.c_void_p * 1)(P)
+    place = dict(bt=2 * P, cu=3 * P, ctx=4 * P, path=5 * P, n=6 * P)  # 40 lanes, 4 blocks each, 100 rows
+    size = dict(bt=640, cu=164, ctx=160, path=400, n=160)
+    for name, at in place.items():
+        for new in (at, at - 156, at + size[name] - 4):
+            a = dict(k=arr, v=arr, L=1, bt=2 * P, mb=4, cu=3 * P, ctx=4 * P, path=5 * P, n=6 * P, new=new, B=40,
+                     T=100, NB=8, bs=16, Hkv=2, D=64, dt=1, st=None, stream=None)
+            assert lib.pa_compact_kv(*a.values()) == 1, (name, new - at)
