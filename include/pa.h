@@ -475,6 +475,10 @@ pa_status pa_attention_static_scratch(const void* q, const void* k_cache, const 
  *               (-1 <= parent < own index). A chain (parent = index - 1) is an
  *               ordinary causal chunk.
  * PA_TREE_MAX_NODES  nodes a lane may have.
+ *
+ * In these operators an array that does not start on a boundary of its elements
+ * (q, out, caches, new rows and probabilities: of 16 bytes) returns
+ * PA_ERR_INVALID_ARG.
  */
 #define PA_TREE_MAX_NODES 256
 /* Splits a lane's keys are cut into at most (see pa_attention_tree). */

@@ -2,6 +2,7 @@
 // launch sequencing. Declarations and contracts are in include/pa.h.
 #include <cfloat>
 #include <cstring>
+#include <initializer_list>
 
 #include "pa_host.cuh"
 #include "pa_pages.cuh"
@@ -123,7 +124,12 @@ bool encode_tree_pieces_map(CUtensorMap* map, const void* q, int T, int H, int D
   return r == CUDA_SUCCESS;
 }
 
-bool aligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
+// 32-bit arrays (NULL is)
+bool aligned4(std::initializer_list<const void*> ptrs) {
+  for (const void* a : ptrs)
+    if (reinterpret_cast<uintptr_t>(a) & 3u) return false;
+  return true;
+}
 
 // Whether two arrays share a byte.
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -201,7 +207,9 @@ pa_status pa_attention_tree(const void* q, const void* k_cache, const void* v_ca
     return PA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
     return PA_ERR_INVALID_ARG;
-  if (with_write && (!aligned16(k_new) || !aligned16(v_new))) return PA_ERR_INVALID_ARG;
+  if (!aligned4({block_tables, cu_seqlens_q, ctx_lens, tree_parents, status})) return PA_ERR_INVALID_ARG;
+  if (with_write && (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u)))
+    return PA_ERR_INVALID_ARG;
   const int g = H / Hkv;
   const long long ns = max_tree_splits(max_ctx_len, dtype);
   if (((long long)max_q_len * H + 7) / 8 * B > 0x7fffffffLL || ((long long)T * H + 7) / 8 > 0x7fffffffLL ||
@@ -313,10 +321,8 @@ pa_status pa_verify_tree(const float* target_probs, const float* draft_probs,
                 !tokens))
     return PA_ERR_INVALID_ARG;
   if (!aligned16(target_probs) || !aligned16(draft_probs)) return PA_ERR_INVALID_ARG;
-  for (const void* a : {(const void*)draft_tokens, (const void*)tree_parents,
-                        (const void*)cu_seqlens_q, (const void*)u_accept, (const void*)u_sample,
-                        (const void*)n_accepted, (const void*)path, (const void*)tokens})
-    if (!aligned4(a)) return PA_ERR_INVALID_ARG;
+  if (!aligned4({draft_tokens, tree_parents, cu_seqlens_q, u_accept, u_sample, n_accepted, path, tokens, status}))
+    return PA_ERR_INVALID_ARG;
   VerifyParams p;
   p.p = target_probs;
   p.q = draft_probs;
@@ -352,6 +358,8 @@ pa_status pa_compact_kv(void* const* k_caches, void* const* v_caches, int32_t la
   if (B == 0 || layers == 0) return layers == 0 && B > 0 ? PA_ERR_INVALID_ARG : PA_OK;
   if (!k_caches || !v_caches || !block_tables || !cu_seqlens_q || !ctx_lens || !path ||
       !n_accepted || !new_ctx_lens || max_blocks_per_seq <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned4({block_tables, cu_seqlens_q, ctx_lens, path, n_accepted, new_ctx_lens, status}))
     return PA_ERR_INVALID_ARG;
   // several CTAs, and the launches of further layers, read a lane's lengths and
   // path after one of them has written its new length
@@ -394,7 +402,7 @@ pa_status pa_copy_blocks(void* const* k_caches, void* const* v_caches, int32_t l
   if (st != PA_OK) return st;
   if ((long long)num_blocks * block_size > 0x7fffffffLL || n > (1 << 16)) return PA_ERR_UNSUPPORTED;
   if (n == 0 || layers == 0) return PA_OK;
-  if (!k_caches || !v_caches || !pairs || (reinterpret_cast<uintptr_t>(pairs) & 7u))
+  if (!k_caches || !v_caches || !pairs || (reinterpret_cast<uintptr_t>(pairs) & 7u) || !aligned4({status}))
     return PA_ERR_INVALID_ARG;
   st = check_caches(k_caches, v_caches, layers);
   if (st != PA_OK) return st;

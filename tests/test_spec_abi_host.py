@@ -170,3 +170,22 @@ def test_compact_wants_its_output_apart(lib):
             a = dict(k=arr, v=arr, L=1, bt=2 * P, mb=4, cu=3 * P, ctx=4 * P, path=5 * P, n=6 * P, new=new, B=40,
                      T=100, NB=8, bs=16, Hkv=2, D=64, dt=1, st=None, stream=None)
             assert lib.pa_compact_kv(*a.values()) == 1, (name, new - at)
+
+
+def test_arrays_off_their_elements_boundary(lib):
+    """A 32-bit (64-bit) array that does not start on a 4 (8) byte boundary would fault in a kernel: refused."""
+    for name in ("bt", "cu", "ctx", "par", "st"):
+        for off in (1, 2):
+            assert tree(lib, **{name: P + off}) == 1, name
+    assert tree(lib, slot=P + 4, kn=P, vn=P) == 1
+    verify = dict(p=P, q=P, tok=P, par=P, cu=P, ua=P, us=P, n=P, path=P, out=P, B=1, T=4, V=100, mq=4, st=P,
+                  stream=None)
+    for name in ("tok", "par", "cu", "ua", "us", "n", "path", "out", "st"):
+        assert lib.pa_verify_tree(*dict(verify, **{name: P + 2}).values()) == 1, name
+    arr = (ctypes.c_void_p * 1)(P)
+    compact = dict(k=arr, v=arr, L=1, bt=P, mb=4, cu=P, ctx=P, path=P, n=P, new=2 * P, B=1, T=1, NB=8, bs=16, Hkv=2,
+                   D=64, dt=1, st=P, stream=None)
+    for name in ("bt", "cu", "ctx", "path", "n", "new", "st"):
+        assert lib.pa_compact_kv(*dict(compact, **{name: compact[name] + 2}).values()) == 1, name
+    copy = dict(k=arr, v=arr, L=1, pairs=P, n=1, NB=8, bs=16, Hkv=2, D=64, dt=1, st=P + 2, stream=None)
+    assert lib.pa_copy_blocks(*copy.values()) == 1
