@@ -22,7 +22,6 @@
 namespace pa {
 
 constexpr int kTreeMaxNodes = PA_TREE_MAX_NODES;
-constexpr int kTreeTile = 128;  // keys per tile of the walk
 // (row, head) pairs of one kv head that a row tile holds: M of the products
 constexpr int kTreeRows = 128;
 

@@ -639,10 +639,6 @@ cudaError_t launch_verify(const VerifyParams& p, cudaStream_t s) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (ranks > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   return cudaLaunchKernelEx(&cfg, verify_kernel, p);
 }
 
