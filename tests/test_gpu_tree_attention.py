@@ -530,3 +530,69 @@ def test_a_bound_of_no_rows_is_raised(dtype, ctx):
     out, flags = s.run(max_q_len=0, max_ctx_len=ctx)
     assert flags == pa.FLAGS["HOST_BOUND"]
     assert torch.isnan(out).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("past", [40, 1500])
+def test_values_not_finite_in_any_tile(dtype, past):
+    """As above in trees of several row tiles and key tiles, and for the codes of NaN: element 5 of the
+    rows that attend such a node is what the formula gives, the rest of them and every other row as with
+    finite values."""
+    rng = np.random.default_rng(past)
+    lanes = [(past, sh.tree(rng, 140)), (past + 3, sh.chain(30)), (past + 9, sh.forest(rng, 200))]
+    s = sh.Step(lanes, 8, 2, 128, 16, dtype, seed=22)
+    clean, _ = s.run()
+    odd = {}
+    for b, (p, par) in enumerate(lanes):
+        for j in rng.choice(len(par), 5, replace=False).tolist() + [len(par) - 1]:
+            i, r = s.row(b, p + j)
+            value = float(rng.choice([np.nan, np.inf, -np.inf])) if dtype != "fp8" else int(rng.choice([0x7F, 0xFF]))
+            s.v[i, r, 1, 5] = value
+            odd[int(s.cu[b]) + j] = value if dtype != "fp8" else float("nan")
+    got, flags = s.run()
+    assert flags == 0
+    import oracle.speculative as osp
+    want, hit = clean.clone(), 0
+    for b, (p, par) in enumerate(lanes):
+        for j in range(len(par)):
+            met = [odd[int(s.cu[b]) + a] for a in osp.ancestors(par, j) if int(s.cu[b]) + a in odd]
+            if met:
+                hit += 1
+                want[int(s.cu[b]) + j, 4:, 5] = sum(met)
+    assert 0 < hit < s.T
+    assert torch.equal(torch.nan_to_num(got, nan=12345.0), torch.nan_to_num(want, nan=12345.0))
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "f32"])
+def test_a_graph_of_each_type(dtype):
+    """Captured and replayed on changed inputs, as the eager call gives them."""
+    s = sh.Step(lanes_of(6, [(1500, 6, "tree"), (64, 20, "tree")]), 8, 2, 128, 16, dtype, seed=13)
+    dev = s.to_device()
+    want, _ = s.run(dev)
+    args = [dev[k] for k in ("q", "k_cache", "v_cache", "block_tables", "cu_seqlens_q", "ctx_lens", "tree_parents")]
+    g, out, ws = torch.cuda.CUDAGraph(), torch.full_like(want, float("nan")), s.workspace()
+    with torch.cuda.graph(g):
+        pa.attention_tree(*args, out, workspace=ws, **s.kwargs())
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    dev["q"].copy_(torch.flip(dev["q"], [0]))
+    dev["ctx_lens"].copy_(torch.tensor([700, 64], dtype=torch.int32))
+    g.replay()
+    now, _ = s.run(dev)
+    assert torch.equal(out, now) and not torch.equal(now, want)
+
+
+def test_an_e4m3_chain_is_a_causal_chunk():
+    """Over e4m3 caches a chain gives what pa_attention gives for the chunk, within both kernels' bound."""
+    s = sh.Step([(700, sh.chain(30)), (10, sh.chain(1)), (2000, sh.chain(100))], 8, 2, 128, 16, "fp8", seed=6)
+    dev = s.to_device()
+    out, _ = s.run(dev)
+    ref = torch.full_like(out, float("nan"))
+    mq, mc = max(s.n), int(s.ctx.max())
+    n = pa.workspace_bytes(s.B, s.T, mq, mc, -1, 8, 2, 128, 16, s.kind)
+    pa.attention(dev["q"], dev["k_cache"], dev["v_cache"], dev["block_tables"], dev["cu_seqlens_q"],
+                 dev["ctx_lens"], ref, max_q_len=mq, max_ctx_len=mc, scale=s.scale, k_scale=s.k_scale,
+                 v_scale=s.v_scale, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+    s.check(out)
+    s.check(ref)
