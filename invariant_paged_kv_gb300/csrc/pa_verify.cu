@@ -426,14 +426,36 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
     else
       slice(Count<2>());
     long long mine_fix = sums.total();
+    bool took = false;
     if (!with_q) {
       // tokens taken out of the row: each once, by the thread that added it
       for (int k = 0; k < n_rej; ++k) {
         const int x = sm.gone[k], grp = (x + skew) >> 2;
         bool again = false;
         for (int j = 0; j < k; ++j) again |= sm.gone[j] == x;
-        if (!again && grp / 32 / iters == gw && (grp & 31) == lane)
+        if (!again && grp / 32 / iters == gw && (grp & 31) == lane) {
           mine_fix -= (long long)to_fix(p.p[row_at + x]);
+          took = true;
+        }
+      }
+    }
+    float fs, fs1, qs, qs1;
+    f32x2_split(psum, fs, fs1);
+    f32x2_split(qsum, qs, qs1);
+    fs += fs1;
+    // (rare) next to nothing is left, and it may be no more than what the sums
+    // rounded: 2^-58 beside each token taken out, 2^-47 of p where p is A q. The
+    // draw must not land on what is not there, so such a thread sums its entries
+    // anew, as the draw reads them. (After one rejection with draft rows every
+    // difference is exact, and what is left of it is there.)
+    if (mine_fix > 0 && (with_q ? n_rej >= 2 && (float)mine_fix < fs * 0x1p17f : took && mine_fix < (1 << 17))) {
+      mine_fix = 0;
+      for (int i = 0; i < iters; ++i) {
+        float4 pv, qv;
+        load(g0 + 32 * i, pv, qv);
+        u64 r[4];
+        fix(g0 + 32 * i, pv, qv, r);
+        mine_fix += (long long)((r[0] + r[1]) + (r[2] + r[3]));
       }
     }
     const u64 total_w = warp_sum((u64)(mine_fix > 0 ? mine_fix : 0));
@@ -447,10 +469,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
                  prob_ok(qv.y) && prob_ok(qv.z) && prob_ok(qv.w));
       }
     }
-    float fs, fs1, qs, qs1;
-    f32x2_split(psum, fs, fs1);
-    f32x2_split(qsum, qs, qs1);
-    fs = warp_sum_f(fs + fs1);
+    fs = warp_sum_f(fs);
     qs = warp_sum_f(qs + qs1);
     if (lane == 0) {
       sm.wsum[warp] = total_w;

@@ -426,3 +426,43 @@ def test_draws_within_a_hair_of_a_running_sum(V, lanes, drafts):
                      np.array([r[3] for r in rows], np.float32))
     assert flags == 0 and (got[0] == 0).all()
     np.testing.assert_array_equal(got[2][::n], [r[4] for r in rows])
+
+
+@pytest.mark.parametrize("V", [300, 2500, 40000])
+def test_a_draw_of_zero_takes_the_first_entry_that_is_left(V):
+    """u_sample = 0 over rows that are nearly all zeros: tokens taken out, of any size and with any last
+    bits, leave nothing behind that could be drawn in their place."""
+    rng = np.random.default_rng(V)
+    lanes, n = 64, 6
+    p = np.zeros((lanes * n, V), np.float32)
+    tokens = np.zeros(lanes * n, np.int32)
+    want = []
+    for b in range(lanes):
+        places = np.sort(rng.choice(V - 40, n - 1, replace=False))
+        p[b * n, places] = 2.0 ** -rng.uniform(20, 45, n - 1) * rng.uniform(1, 2, n - 1)
+        p[b * n, V - 40 + b % 40] = 0.9
+        tokens[b * n + 1:b * n + n] = places
+        want.append(V - 40 + b % 40)
+    u, us = np.full(lanes * n, 0.999, np.float32), np.zeros(lanes, np.float32)
+    got, flags = run(p, None, tokens, [[-1] + [0] * (n - 1)] * lanes, u, us)
+    assert flags == 0 and (got[0] == 0).all()
+    np.testing.assert_array_equal(got[2][::n], want)
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("V", [130, 700])
+def test_draws_at_the_ends_of_cut_rows(V, drafts):
+    """Rows of a few entries of all sizes, several rejections, u_sample 0 and next to 1: exactly as by
+    rationals."""
+    rng = np.random.default_rng(V)
+    trees = [[-1] + [0] * int(rng.integers(1, 6)) for _ in range(60)]
+    p, q, tokens, u, us = make(V, trees, V, 1.0, 6.0)
+    cut = rng.random(p.shape) < 0.97
+    cut[np.arange(len(p)), p.argmax(-1)] = False
+    p = np.where(cut, np.float32(0), p)
+    u[:] = np.float32(1 - 2.0 ** -24)
+    us[::2], us[1::2] = 0, 1 - 2.0 ** -24
+    q = q if drafts else None
+    got, flags = run(p, q, tokens, trees, u, us)
+    assert flags == 0
+    same(got, osp.verify_tree(p, q, tokens, np.array([x for t in trees for x in t]), cu_of(trees), u, us, exact=True))
