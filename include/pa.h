@@ -518,8 +518,9 @@ size_t pa_tree_workspace_bytes(int32_t B, int32_t T, int32_t max_q_len, int32_t 
  * q_len, each reduced in ascending key order, and folded left to right in
  * fp32. bf16 steps multiply on the tensor cores in bf16, with p rounded to
  * bf16. e4m3 steps multiply the codes as they are, q and p as sums of 8-bit
- * values: q to 2^-17 of its row's largest element, p to 9 significant bits.
- * fp32 steps multiply and add in fp32.
+ * values: q to 2^-17 of its row's largest element, p to 9 significant bits
+ * (pa_attention keeps 11 of p over the same caches). fp32 steps multiply and add
+ * in fp32. The same token in another tree, or through pa_attention, has other bits.
  *
  * workspace: pa_tree_workspace_bytes(...) bytes, 256-byte aligned; contents
  * on entry are irrelevant, calls whose work may overlap on the GPU need
