@@ -568,8 +568,9 @@ pa_status pa_attention_tree(const void* q, const void* k_cache, const void* v_ca
  * if u Z < r(x_c), else r(x_c) = 0 and Z is less by it. Drawn so, a node's
  * token has the target's distribution.
  *
- * Sums are exact to vocab 2^-58 of a row, from a node's second rejection on to
- * another 2^-46 for each, and a lane's results do not depend on the other lanes
+ * Sums are exact to vocab 2^-58 of a row (so entries under that may be passed
+ * over by a u_sample of 0), from a node's second rejection on to another 2^-46
+ * for each, and a lane's results do not depend on the other lanes
  * or on the step. A tree that is none raises PA_FLAG_TREE.
  * Rows read, the target's or the draft's, that hold a value outside [0, 2) or
  * sum to 2 or more (found from 1.99 on) or to under 2^-40, a u_sample and a used
