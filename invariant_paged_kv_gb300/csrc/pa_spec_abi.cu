@@ -356,7 +356,7 @@ pa_status pa_compact_kv(void* const* k_caches, void* const* v_caches, int32_t la
   if ((long long)num_blocks * block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
   if (T > 0 && B == 0) return PA_ERR_INVALID_ARG;
   if (B == 0 || layers == 0) return layers == 0 && B > 0 ? PA_ERR_INVALID_ARG : PA_OK;
-  if (!k_caches || !v_caches || !block_tables || !cu_seqlens_q || !ctx_lens || !path ||
+  if (!k_caches || !v_caches || !block_tables || !cu_seqlens_q || !ctx_lens || (T > 0 && !path) ||
       !n_accepted || !new_ctx_lens || max_blocks_per_seq <= 0)
     return PA_ERR_INVALID_ARG;
   if (!aligned4({block_tables, cu_seqlens_q, ctx_lens, path, n_accepted, new_ctx_lens, status}))

@@ -239,3 +239,15 @@ def test_streams_and_graphs():
     np.testing.assert_array_equal(out.cpu().numpy(), new)
     for a, b in zip(raw(k + v), want):
         np.testing.assert_array_equal(a, b)
+
+
+def test_compact_a_step_without_rows():
+    """Lanes and no row at all (an empty path has no address): the lengths are passed on."""
+    k, v = layers(2, 6, 16, 2, 64, "bf16")
+    before = raw(k + v)
+    s = dict(tables=np.arange(6, dtype=np.int32).reshape(3, 2), cu=np.zeros(4, np.int32),
+             ctx=np.array([0, 17, 32], np.int32), path=np.zeros(0, np.int32), keep=np.full(3, -1, np.int32))
+    new, flags = compact(k, v, s)
+    assert flags == 0 and new.tolist() == [0, 17, 32]
+    for a, b in zip(raw(k + v), before):
+        np.testing.assert_array_equal(a, b)
